@@ -27,8 +27,10 @@ __device__ __forceinline__ float seen(float m, float l) { return l != l && m == 
 // what counts is bytes in flight (8 KB per warp and stage at d = 128; two stages and three CTAs per SM read 5.6 TB/s of
 // 4 x 64 x 16 windows of 512, 194 us, three stages and two CTAs 5.2 TB/s).  A warp looks 32 tiles' pages up at once (4 x
 // 32 x 4 key heads of 64: 140 us, page by page 162).  P enters the
-// product as two bf16 numbers, so that the weights keep 15 bits: the output's own rounding stays the
-// largest error, and the extra products cost nothing under the loads.
+// product as three bf16 numbers, which hold all its bits (swa_decode_common.cuh).  A group of up to 8 heads leaves the
+// lower half of the 16 rows empty (R = 1): there the second parts take it, beside the first ones, and O is the sum of
+// both halves in the end; so two products do, and half of the exponentials.  The tensor core cuts its fp32 sums
+// instead of rounding them (O lost up to 2^-17 of itself over 64 tiles), so each tile's product starts from zero.
 template <int DP> struct Ring {
     static constexpr int kHalf = 16 * DP * 2;            // 16 rows of K (or V), bytes
     static constexpr int kStage = 2 * kHalf;
@@ -50,7 +52,16 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int DP, int W, int ST>
+// The same from zero.
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+                 "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+template <int DP, int W, int ST, int R>
 __global__ void __launch_bounds__(32 * W) swa_decode_kernel(const __grid_constant__ Params p)
 {
     constexpr int KS = DP / 16;                          // steps of 16 along d
@@ -158,7 +169,12 @@ __global__ void __launch_bounds__(32 * W) swa_decode_kernel(const __grid_constan
     for (int k = 0; k < 2 * KS; ++k)
         #pragma unroll
         for (int f = 0; f < 4; ++f) o[k][f] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float m[R], l[R];
+    #pragma unroll
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+    }
 
     int stage = 0;
     for (int64_t i = i0 + warp; i < i1; i += W) {
@@ -184,16 +200,16 @@ __global__ void __launch_bounds__(32 * W) swa_decode_kernel(const __grid_constan
         #pragma unroll
         for (int j = 0; j < 2; ++j)
             #pragma unroll
-            for (int f = 0; f < 4; ++f) {
+            for (int f = 0; f < 2 * R; ++f) {
                 const int col = 8 * j + 2 * (lane & 3) + (f & 1);
                 s[j][f] = col >= c_lo && col < c_hi ? s[j][f] * p.xscale : -INFINITY;
             }
         // the reference maximum of a row is raised only when a tile exceeds it by more than 8 (so
         // weights stay below 2^8); O and the sum then shrink
-        float corr[2];
+        float corr[R];
         bool raised = false;
         #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < R; ++r) {
             float bm = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
@@ -205,41 +221,59 @@ __global__ void __launch_bounds__(32 * W) swa_decode_kernel(const __grid_constan
             }
         }
         if (__any_sync(0xffffffffu, raised)) {
-            l[0] *= corr[0];
-            l[1] *= corr[1];
+            #pragma unroll
+            for (int r = 0; r < R; ++r) l[r] *= corr[r];
             #pragma unroll
             for (int k = 0; k < 2 * KS; ++k) {
                 o[k][0] *= corr[0];
                 o[k][1] *= corr[0];
-                o[k][2] *= corr[1];
-                o[k][3] *= corr[1];
+                o[k][2] *= corr[R - 1];
+                o[k][3] *= corr[R - 1];
             }
         }
-        uint32_t ph[4], pl[4];
+        uint32_t ph[4], pm[4], pl[4];
         #pragma unroll
         for (int j = 0; j < 2; ++j)
             #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int r = 0; r < R; ++r) {
                 const float ms = m[r] == -INFINITY ? 0.f : m[r];
                 const float p0 = ex2(s[j][2 * r] - ms), p1 = ex2(s[j][2 * r + 1] - ms);
                 l[r] += p0 + p1;
-                split_bf16(p0, p1, ph[2 * j + r], pl[2 * j + r]);
+                if constexpr (R == 1) {
+                    split_bf16(p0, p1, ph[2 * j], ph[2 * j + 1], pl[2 * j], 0.5f);
+                    pl[2 * j + 1] = pl[2 * j];
+                } else {
+                    split_bf16(p0, p1, ph[2 * j + r], pm[2 * j + r], pl[2 * j + r], 1.f);
+                }
             }
         #pragma unroll
         for (int k = 0; k < KS; ++k) {
             const uint32_t key = (lane & 7) + ((lane >> 3) & 1) * 8, ch = 2 * k + (lane >> 4);
             uint32_t bf[4];
             sm100::ldsm_x4_trans(vt + key * (DP * 2) + ((ch ^ (key & 7)) << 4), bf);
-            mma_bf16(o[2 * k], ph, bf[0], bf[1]);
-            mma_bf16(o[2 * k + 1], ph, bf[2], bf[3]);
-            mma_bf16(o[2 * k], pl, bf[0], bf[1]);
-            mma_bf16(o[2 * k + 1], pl, bf[2], bf[3]);
+            // the tensor core cuts its sums, so a tile's product starts from zero and is added to O rounded to nearest
+            float t[2][4];
+            #pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                mma_bf16_first(t[n], pl, bf[2 * n], bf[2 * n + 1]);
+                if constexpr (R == 2) mma_bf16(t[n], pm, bf[2 * n], bf[2 * n + 1]);
+                mma_bf16(t[n], ph, bf[2 * n], bf[2 * n + 1]);
+                #pragma unroll
+                for (int f = 0; f < 4; ++f) o[2 * k + n][f] += t[n][f];
+            }
         }
         __syncwarp();                                    // every lane is done with the stage
     }
     cp_async_wait<0>();
+    if constexpr (R == 1) {
+        #pragma unroll
+        for (int k = 0; k < 2 * KS; ++k) {
+            o[k][0] += o[k][2];
+            o[k][1] += o[k][3];
+        }
+    }
     #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < R; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         m[r] = seen(m[r], l[r]);
@@ -249,7 +283,7 @@ __global__ void __launch_bounds__(32 * W) swa_decode_kernel(const __grid_constan
     float* so = reinterpret_cast<float*>(smem);          // [W][16][DP]
     float2* sm = reinterpret_cast<float2*>(smem + W * 16 * DP * 4);
     #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < R; ++r) {
         const int row = (lane >> 2) + 8 * r;
         if ((lane & 3) == 0) sm[warp * 16 + row] = make_float2(m[r], l[r]);
         if (row < rows) {
@@ -528,7 +562,9 @@ cudaError_t launch(K kernel, const Params& p, dim3 grid, size_t smem, bool early
 template <int DP, int W, int ST>
 cudaError_t launch_tc(const Params& p, dim3 grid, bool early, cudaStream_t stream)
 {
-    return launch(swa_decode_kernel<DP, W, ST>, p, grid, W * ST * Ring<DP>::kStage, early, stream, 32 * W);
+    const size_t smem = W * ST * Ring<DP>::kStage;
+    return p.c.Hq / p.c.Hkv <= 8 ? launch(swa_decode_kernel<DP, W, ST, 1>, p, grid, smem, early, stream, 32 * W)
+                                 : launch(swa_decode_kernel<DP, W, ST, 2>, p, grid, smem, early, stream, 32 * W);
 }
 
 // As many rows in a CTA's registers as the group has heads (1, 2 or 4), and no more elements than the width needs.
@@ -589,12 +625,21 @@ DecodePlan plan_decode(const DecodeCall& c)
     return plan;
 }
 
+// A shared prefix's sums between two runs, 64 KB for a CTA, where one may have more than a run of blocks.
+static size_t between_bytes(const DecodeCall& c, const DecodePlan& plan)
+{
+    if (plan.prefix_splits == 0) return 0;
+    const int64_t blocks = (c.prefix / 64 + plan.prefix_splits - 1) / plan.prefix_splits;
+    if (blocks <= swad::kPrefixRun) return 0;
+    return static_cast<size_t>(c.T * c.Hkv * plan.tiles) * plan.prefix_splits * (128 * 128 * 4);
+}
+
 size_t decode_workspace_bytes(const DecodeCall& c)
 {
     const DecodePlan plan = plan_decode(c);
     if (plan.slots() <= 1) return 0;               // (a shared prefix makes two at least)
     const size_t rows = static_cast<size_t>(c.T * c.B * c.Hq) * plan.slots();
-    return (rows * 8 + 15) / 16 * 16 + rows * c.d * 4;
+    return (rows * 8 + 15) / 16 * 16 + rows * c.d * 4 + between_bytes(c, plan);
 }
 
 cudaError_t launch_swa_decode(const DecodeCall& c, cudaStream_t stream)
@@ -609,6 +654,7 @@ cudaError_t launch_swa_decode(const DecodeCall& c, cudaStream_t stream)
     const size_t rows = static_cast<size_t>(c.T * c.B * c.Hq);
     p.ml = reinterpret_cast<float2*>(c.workspace);
     p.acc = p.slots ? c.workspace + (rows * p.slots * 8 + 15) / 16 * 4 : nullptr;
+    p.between = between_bytes(c, p.plan) ? p.acc + rows * p.slots * c.d : nullptr;
     const dim3 grid(static_cast<unsigned>(c.T * c.Hkv * c.B * p.plan.group_tiles), p.plan.own_splits);
     cudaError_t e;
     if (p.plan.prefix_splits > 0) {
