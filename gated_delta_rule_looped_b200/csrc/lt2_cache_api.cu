@@ -49,6 +49,7 @@ lt2_status fill_turns(const lt2_rope* r, int64_t d, lt2::AppendCall* c)
     c->interleaved = 0;
     if (!r || r->rot_dim == 0) return LT2_OK;
     if (r->rot_dim < 0 || r->rot_dim % 2 != 0 || r->rot_dim > d) return LT2_ERR_INVALID_ARGUMENT;
+    if (r->rot_dim / 2 > lt2::kMaxRotPairs) return LT2_ERR_UNSUPPORTED;    // more than the tables below hold
     if (r->interleaved != 0 && r->interleaved != 1) return LT2_ERR_INVALID_ARGUMENT;
     if (!r->inv_freq && !(r->base > 0.0 && std::isfinite(r->base))) return LT2_ERR_INVALID_ARGUMENT;
     c->rot_pairs = r->rot_dim / 2;
@@ -147,11 +148,11 @@ lt2_status lt2_kv_append(const lt2_kv_dims* d, const lt2_rope* rope, const void*
     if (d->d < 1 || d->d >= kMaxDim || d->reserved != 0) return LT2_ERR_INVALID_ARGUMENT;
     if (d->dtype != LT2_DTYPE_F32 && d->dtype != LT2_DTYPE_BF16) return LT2_ERR_INVALID_ARGUMENT;
     if (!cu_seqlens && d->N != d->B) return LT2_ERR_INVALID_ARGUMENT;
+    const int shift = page_shift(d->page_size);
+    if (shift < 0 || d->d > 256) return LT2_ERR_UNSUPPORTED;
     lt2::AppendCall c = {};
     st = fill_turns(rope, d->d, &c);
     if (st != LT2_OK) return st;
-    const int shift = page_shift(d->page_size);
-    if (shift < 0 || d->d > 256) return LT2_ERR_UNSUPPORTED;
     int64_t nq, nk, ncache, ntable, rows;
     if (!product_ok({d->T, d->N, d->Hq, d->d}, &nq) || !product_ok({d->T, d->N, d->Hkv, d->d}, &nk) ||
         !product_ok({d->T, d->pages, d->Hkv, d->page_size, d->d}, &ncache) || !product_ok({d->B, d->max_pages}, &ntable))
