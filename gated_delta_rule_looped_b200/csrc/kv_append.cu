@@ -81,8 +81,9 @@ __device__ __forceinline__ Vec<T> turn_pairs(const Vec<T>& a, const float2* t, i
     return Vec<T>::of(x);
 }
 
-// The sequence that packed token n belongs to, or -1 (before the first or behind the last one).
-__device__ __forceinline__ int64_t sequence_of(const int64_t* cu, int64_t B, int64_t n)
+// The sequence that packed token n of N belongs to, and its place there; -1 where it belongs to none (before the first or
+// behind the last one) or to one with a bad offset: below 0, past N, or out of order with a neighbour.
+__device__ __forceinline__ int64_t sequence_of(const int64_t* cu, int64_t B, int64_t N, int64_t n, int64_t& i)
 {
     int64_t lo = 0, hi = B;                        // the last b in [0, B] with cu[b] <= n, if any
     if (cu[0] > n) return -1;
@@ -90,7 +91,12 @@ __device__ __forceinline__ int64_t sequence_of(const int64_t* cu, int64_t B, int
         const int64_t mid = (lo + hi + 1) >> 1;
         if (cu[mid] <= n) lo = mid; else hi = mid - 1;
     }
-    return lo < B && cu[lo + 1] > n ? lo : -1;
+    if (lo == B) return -1;
+    const int64_t first = cu[lo], end = cu[lo + 1];
+    if (first < 0 || first > n || end <= n || end > N) return -1;
+    if ((lo > 0 && cu[lo - 1] > first) || (lo + 2 <= B && cu[lo + 2] < end)) return -1;
+    i = n - first;
+    return lo;
 }
 
 // A row's two or three places: source, destination, and a second destination (k_out beside the cache row).
@@ -171,10 +177,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
         const int64_t n = n0 + threadIdx.x;
         int64_t at = -1, pos = 0;
         if (n < c.N) {
-            const int64_t b = c.cu ? sequence_of(c.cu, c.B, n) : n;
+            int64_t i = 0;
+            const int64_t b = c.cu ? sequence_of(c.cu, c.B, c.N, n, i) : n;
             if (b >= 0) {
                 const int64_t first = c.start[b], cap = c.max_pages << c.page_shift;
-                const int64_t i = c.cu ? n - c.cu[b] : 0;
                 if (first < 0 || first >= cap || i >= cap - first) {
                     atomicOr(c.err, kDevSeqlens);
                 } else {

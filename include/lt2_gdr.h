@@ -399,9 +399,11 @@ typedef struct lt2_kv_dims {
  *               outside every sequence are left alone
  *   q_out       rotated q, layout of q (may equal q exactly: in place)
  *   k_out       rotated k, layout of k (may equal k exactly), or NULL: only the cache is written
- * Two sequences must not append to the same page.  A position that the page table does not hold, or
- * bad offsets, record LT2_ERR_SEQLENS, a page outside the cache LT2_ERR_PAGES; nothing is written for
- * such a token.  No workspace.  Return convention of lt2_gdr_prefill; LT2_ERR_UNSUPPORTED for other
+ * Two sequences must not append to the same page.  A position that the page table does not hold
+ * records LT2_ERR_SEQLENS, a page outside the cache LT2_ERR_PAGES; nothing is written for such a token.
+ * An offset below 0, past N or out of order with a neighbour records LT2_ERR_SEQLENS too, and the
+ * sequences on both its sides are left unwritten (the others arrive; a token that two of them claim
+ * goes to one of them).  No workspace.  Return convention of lt2_gdr_prefill; LT2_ERR_UNSUPPORTED for other
  * page sizes and d > 256.
  */
 lt2_status lt2_kv_append(const lt2_kv_dims* dims, const lt2_rope* rope,
