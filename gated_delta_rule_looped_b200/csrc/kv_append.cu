@@ -5,8 +5,8 @@
 //
 // An angle at position 10^6 loses its fraction in fp32 (a step of fp32 is 0.06 rad there), so positions are
 // turned into fractions of a turn in 64-bit fixed point: frequency / 2 pi is an integer number of
-// 2^-64 turns, its product with the position wraps modulo whole turns exactly, and only the
-// remainder becomes a float (at most 2^-25 turns off).
+// 2^-64 turns, its product with the position wraps modulo whole turns exactly, and the remainder's
+// cosine and sine are taken in fp64, once for all loops and heads, and rounded once.
 //
 // CTA = up to 8 tokens and a share of their (loop, head) rows.  The tokens' cos and sin go to shared
 // memory once and serve every loop and head; a thread then moves two 16-byte vectors of a row, the two halves of
@@ -200,10 +200,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     for (int i = threadIdx.x; i < p.tokens * c.rot_pairs; i += kThreads) {
         const int tk = i / c.rot_pairs, j = i - tk * c.rot_pairs;
         const uint64_t turn = c.turns[j] * static_cast<uint64_t>(posn[tk]);
-        const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873e-10f;   // 2^-31
-        float s, co;
-        sincospif(half_turns, &s, &co);
-        cs[tk][j] = make_float2(co, s);
+        double s, co;
+        sincospi(static_cast<double>(static_cast<int64_t>(turn)) * 0x1p-63, &s, &co);      // in half turns
+        cs[tk][j] = make_float2(static_cast<float>(co), static_cast<float>(s));
     }
     __syncthreads();
 
