@@ -174,8 +174,9 @@ __global__ void __launch_bounds__(kSplitThreads) glr_split_backward_map_kernel(c
     put_map<PAIR>(p, s, A, M);
 }
 
-// A warp per channel: lane j folds a run of segments, the lanes' maps are composed in a fixed order, and each lane
-// passes its carry over its run.  REVERSE: from the last segment to the first.
+// A warp per channel: lane j holds the map of segment j of 32, and the carry passes over them one after another, as it does from
+// tile to tile: a product of maps over more than a segment may overflow where the state itself does not.  REVERSE: from
+// the last segment to the first.
 template <bool REVERSE>
 __global__ void __launch_bounds__(kSplitThreads) glr_split_carry_kernel(const __grid_constant__ SplitParams p)
 {
@@ -186,34 +187,20 @@ __global__ void __launch_bounds__(kSplitThreads) glr_split_carry_kernel(const __
     if (c >= p.channels) return;
     const int64_t unit = c / p.s.d, ch = c - unit * p.s.d;
     const float2* m = p.maps + c * p.segs;
-    const int64_t run = (p.segs + 31) / 32;
-    const int64_t i0 = lane * run < p.segs ? lane * run : p.segs, i1 = i0 + run < p.segs ? i0 + run : p.segs;
     auto at = [&](int64_t i) { return REVERSE ? p.segs - 1 - i : i; };
-    float A = 1.f, H = 0.f;
-    #pragma unroll 4
-    for (int64_t i = i0; i < i1; ++i) {
-        const float2 v = m[at(i)];
-        H = fmaf(v.x, H, v.y);
-        A *= v.x;
-    }
-    // exclusive composition over the lanes in front
-    #pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-        const float a = __shfl_up_sync(0xffffffffu, A, s), h = __shfl_up_sync(0xffffffffu, H, s);
-        if (lane >= s) {
-            H = fmaf(A, h, H);
-            A *= a;
+    auto map_of = [&](int64_t i) { return i < p.segs ? m[at(i)] : make_float2(1.f, 0.f); };
+    float carry = p.first ? p.first[c] : 0.f;
+    float2 next = map_of(lane);
+    for (int64_t i0 = 0; i0 < p.segs; i0 += 32) {
+        const float2 v = next;
+        next = map_of(i0 + 32 + lane);                     // under the chain of this group's
+        float mine = carry;
+        #pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (lane == j) mine = carry;
+            carry = fmaf(__shfl_sync(0xffffffffu, v.x, j), carry, __shfl_sync(0xffffffffu, v.y, j));
         }
-    }
-    A = __shfl_up_sync(0xffffffffu, A, 1);
-    H = __shfl_up_sync(0xffffffffu, H, 1);
-    const float first = p.first ? p.first[c] : 0.f;
-    float carry = lane == 0 ? first : fmaf(A, first, H);
-    #pragma unroll 4
-    for (int64_t i = i0; i < i1; ++i) {
-        const float2 v = m[at(i)];
-        p.carries[(unit * p.segs + at(i)) * p.s.d + ch] = carry;
-        carry = fmaf(v.x, carry, v.y);
+        if (i0 + lane < p.segs) p.carries[(unit * p.segs + at(i0 + lane)) * p.s.d + ch] = mine;
     }
 }
 

@@ -499,8 +499,9 @@ size_t lt2_glr_prefill_workspace_bytes(const lt2_glr_dims* dims);
  *   workspace  lt2_glr_prefill_workspace_bytes(dims) bytes of device scratch (16-byte aligned); its
  *              content need not survive the call, and calls that overlap on the GPU need their own
  * L = 0 copies S0 to S_out.  Results do not depend on timing: the same call gives the same bits.
- * Decays are expected within [-1, 1]; larger ones work while their product over 64 tokens is
- * finite in fp32, and the call records LT2_ERR_RANGE where it is not.  LT2_ERR_UNSUPPORTED for bf16
+ * Decays are expected within [-1, 1]; larger ones work while the product of any 64 in a row is
+ * finite in fp32, and the call records LT2_ERR_RANGE where it multiplied some that are not (a walk
+ * multiplies none).  LT2_ERR_UNSUPPORTED for bf16
  * gates with fp32 x; otherwise the return convention of lt2_gdr_prefill.
  */
 lt2_status lt2_glr_prefill(const lt2_glr_dims* dims,
