@@ -665,21 +665,31 @@ def _scratch(n, like, stream):
     import torch
     if not n:
         return None
-    ws = torch.empty(n, dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        _used_on((ws,), stream)
-    return ws
+    with _memory_of(stream):
+        return torch.empty(n, dtype=torch.uint8, device=like.device)
 
 
-def _used_on(tensors, stream):
-    """Tells the allocator that ``tensors``, made here on the current stream, are used on ``stream``, so
-    that their memory is not handed out again before that stream is done with them."""
+def _memory_of(stream):
+    """Context in which new tensors take their memory from what ``stream`` has to spare (None: the current
+    stream, as always).  Memory that was freed on the current stream may still be in use by work that is
+    queued there, which ``stream`` does not wait for."""
     import torch
-    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-    if s.cuda_stream != torch.cuda.current_stream().cuda_stream:
+    if stream is None:
+        return _NOTHING
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def _hand_out(tensors, stream):
+    """``tensors``, made with the memory of ``stream``, go to a caller on the current stream: once freed, their
+    memory is not used again before that stream is done with them too."""
+    import torch
+    if stream is None:
+        return
+    here = torch.cuda.current_stream()
+    if here.cuda_stream != _stream(stream):
         for t in tensors:
             if t is not None:
-                t.record_stream(s)
+                t.record_stream(here)
 
 
 # --- the paged cache of the sliding-window mixer ---------------------------------------------
@@ -759,9 +769,9 @@ def kv_append(q, k, v, k_cache, v_cache, page_table, start, cu_seqlens=None, rop
                 if rope is None:
                     q_out = q
                 else:
-                    q_out = torch.empty_like(q)
-                    if stream is not None:
-                        _used_on((q_out,), stream)
+                    with _memory_of(stream):
+                        q_out = torch.empty_like(q)
+                    _hand_out((q_out,), stream)
                 pqo = q_out.data_ptr()
             else:
                 pqo = _need("q_out", q_out, qs, dt, k)
@@ -771,9 +781,9 @@ def kv_append(q, k, v, k_cache, v_cache, page_table, start, cu_seqlens=None, rop
             raise ValueError("q_out without q")
         pko = None
         if k_out is True:
-            k_out = torch.empty_like(k)
-            if stream is not None:
-                _used_on((k_out,), stream)
+            with _memory_of(stream):
+                k_out = torch.empty_like(k)
+            _hand_out((k_out,), stream)
             pko = k_out.data_ptr()
         elif k_out is not None:
             pko = _need("k_out", k_out, ks, dt, k)
@@ -810,9 +820,9 @@ def swa_decode(q, k_cache, v_cache, page_table, seq_lens, window=None, prefix_le
         pages, Hkv, size, width, pkc, pvc, table = _need_cache(k_cache, v_cache, page_table, T, None, d, B, q)
         lens = _need("seq_lens", seq_lens, (B,), torch.int64, q)
         if o is None:
-            o = torch.empty_like(q, dtype=_out_of(q, out))
-            if stream is not None:
-                _used_on((o,), stream)
+            with _memory_of(stream):
+                o = torch.empty_like(q, dtype=_out_of(q, out))
+            _hand_out((o,), stream)
             po = o.data_ptr()
         else:
             po = _need("o", o, qs, _out_of(q, out), q)
@@ -868,23 +878,23 @@ def glr_prefill(x, alpha, beta=None, S0=None, gate_logits=False, alpha_scale=1.0
         state = (xs[0], xs[1], xs[2], xs[4])
         p0 = _may("S0", S0, state, f32, x)
         made = []
-        if o is None:
-            o = torch.empty_like(x, dtype=_out_of(x, out))
-            made.append(o)
-        else:
-            _need("o", o, xs, _out_of(x, out), x)
-        if S_out is None:
-            S_out = x.new_empty(state, dtype=f32)
-            made.append(S_out)
-        else:
-            _need("S_out", S_out, state, f32, x)
         states = ps = None
-        if save_states:
-            states = x.new_empty(state[:3] + (-(-xs[3] // GLR_CHUNK), xs[4]), dtype=f32)
-            ps = states.data_ptr()
-            made.append(states)
-        if stream is not None:
-            _used_on(made, stream)
+        with _memory_of(stream):
+            if o is None:
+                o = torch.empty_like(x, dtype=_out_of(x, out))
+                made.append(o)
+            else:
+                _need("o", o, xs, _out_of(x, out), x)
+            if S_out is None:
+                S_out = x.new_empty(state, dtype=f32)
+                made.append(S_out)
+            else:
+                _need("S_out", S_out, state, f32, x)
+            if save_states:
+                states = x.new_empty(state[:3] + (-(-xs[3] // GLR_CHUNK), xs[4]), dtype=f32)
+                ps = states.data_ptr()
+                made.append(states)
+        _hand_out(made, stream)
         dims, n = _glr_dims(xs, x.dtype, alpha.dtype, bool(gate_logits), float(alpha_scale), out, "prefill")
         ws = _scratch(n, x, stream)
         st = lib().lt2_glr_prefill(dims, px, pa, pb, p0, o.data_ptr(), S_out.data_ptr(), ps,
@@ -905,9 +915,9 @@ def glr_decode(x, alpha, beta, S, S_out=None, gate_logits=False, alpha_scale=1.0
         p0 = _need("S", S, xs, f32, x)
         p1 = p0 if S_out is None else _need("S_out", S_out, xs, f32, x)
         if o is None:
-            o = torch.empty_like(x, dtype=_out_of(x, out))
-            if stream is not None:
-                _used_on((o,), stream)
+            with _memory_of(stream):
+                o = torch.empty_like(x, dtype=_out_of(x, out))
+            _hand_out((o,), stream)
             po = o.data_ptr()
         else:
             po = _need("o", o, xs, _out_of(x, out), x)
@@ -936,10 +946,10 @@ def glr_backward(x, alpha, beta, dO, S0=None, dS_L=None, states=None, gate_logit
         pd = _may("dS_L", dS_L, state, f32, x)
         ps = _may("states", states, state[:3] + (-(-xs[3] // GLR_CHUNK), xs[4]), f32, x)
         xt, gt = (f32, f32) if out == "f32" else (x.dtype, alpha.dtype)
-        g = {"dx": torch.empty_like(x, dtype=xt), "dalpha": torch.empty_like(alpha, dtype=gt),
-             "dbeta": None if beta is None else torch.empty_like(beta, dtype=gt), "dS0": x.new_empty(state, dtype=f32)}
-        if stream is not None:
-            _used_on(g.values(), stream)
+        with _memory_of(stream):
+            g = {"dx": torch.empty_like(x, dtype=xt), "dalpha": torch.empty_like(alpha, dtype=gt),
+                 "dbeta": None if beta is None else torch.empty_like(beta, dtype=gt), "dS0": x.new_empty(state, dtype=f32)}
+        _hand_out(g.values(), stream)
         dims, n = _glr_dims(xs, x.dtype, alpha.dtype, bool(gate_logits), float(alpha_scale), out, "backward")
         ws = _scratch(n, x, stream)
         st = lib().lt2_glr_backward(dims, px, pa, pb, p0, ps, pg, pd, g["dx"].data_ptr(), g["dalpha"].data_ptr(),
