@@ -14,10 +14,9 @@
 // bf16: 470 us with logits, 372 us with decays as values, where HBM's copy rate would take 327).
 #include <cuda_runtime.h>
 
-#include <atomic>
-
 #include "gdr_nvtx.h"
 #include "glr_tile.cuh"
+#include "per_device.h"
 
 namespace lt2 {
 namespace glr {
@@ -332,24 +331,23 @@ inline size_t stream_bytes(__int128 chains, int channels)
     return (256 + static_cast<size_t>(chains) * channels * 4 + 255) / 256 * 256;
 }
 
-// CTAs of a kernel that the GPU holds at once.
+// CTAs of a kernel that the current GPU holds at once.
 template <typename K>
-cudaError_t resident_ctas(K kernel, size_t smem, std::atomic<int>& kept, int* out)
+cudaError_t resident_ctas(K kernel, size_t smem, PerDevice& kept, int* out)
 {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    int n = kept.load(std::memory_order_relaxed);
-    if (n == 0) {
-        int dev = 0, sms = 0, per = 0;
-        if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
-            (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+    *out = kept.get(dev, [&]() {
+        int sms = 0, per = 0;
+        if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
             (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kStreamThreads, smem)) != cudaSuccess)
-            return e;
-        n = sms * (per > 0 ? per : 1);
-        kept.store(n, std::memory_order_relaxed);
-    }
-    *out = n;
-    return cudaSuccess;
+            return 0;
+        return sms * (per > 0 ? per : 1);
+    });
+    return e;
 }
 
 template <typename XT, typename GT, bool LOGITS, int CB, bool BACKWARD>
@@ -361,7 +359,7 @@ cudaError_t run_stream(ScanParams p, const Layout& l, void* workspace, cudaStrea
     else
         kernel = glr_stream_kernel<XT, GT, LOGITS, CB>;
     const size_t smem = (BACKWARD ? kBackwardStages<GT, LOGITS> : 2) * Stage<XT, GT, CB, BACKWARD>::kBytes;
-    static std::atomic<int> kept{0};
+    static PerDevice kept;
     int ctas = 0;
     cudaError_t e = resident_ctas(kernel, smem, kept, &ctas);
     if (e != cudaSuccess) return e;
