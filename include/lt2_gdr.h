@@ -481,7 +481,8 @@ typedef struct lt2_glr_dims {
 } lt2_glr_dims;
 
 /* Bytes of device workspace lt2_glr_prefill needs for `dims`: what the parts of a sequence hand
- * on (up to 12 bytes per channel and 64 tokens); 0 where every sequence is walked by one thread
+ * on (at most 12 bytes per channel and 64 tokens, the channels of a unit counted in whole blocks of
+ * 64, and 512 bytes); 0 where every sequence is walked by one thread
  * per four channels (short sequences, large batches) or fits one tile, and for invalid dims.  Pure
  * host function, no CUDA call. */
 size_t lt2_glr_prefill_workspace_bytes(const lt2_glr_dims* dims);
