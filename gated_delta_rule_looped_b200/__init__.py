@@ -651,6 +651,11 @@ def _out_of(x, out):
     return x.dtype if out is None else _out_torch_dtype(x.dtype, out)
 
 
+def _int64(n):
+    """``n`` as a field of 64 bits takes it: numbers past 2^62 either way, which all say the same, become that."""
+    return max(-(1 << 62), min(int(n), 1 << 62))
+
+
 def _dtype_code(dtype):
     import torch
     if dtype is torch.bfloat16:
@@ -699,6 +704,8 @@ def make_rope(rot_dim, base=10000.0, interleaved=False, inv_freq=None):
     (or position * inv_freq[i], rot_dim / 2 numbers), in pairs (i, i + rot_dim / 2) or, ``interleaved``,
     (2 i, 2 i + 1)."""
     f = None
+    if not -(1 << 31) <= int(rot_dim) < 1 << 31:
+        raise ValueError(f"rot_dim must fit 32 bits, got {rot_dim}")
     if inv_freq is not None:
         inv_freq = [float(x) for x in inv_freq]
         if len(inv_freq) != int(rot_dim) // 2:
@@ -826,8 +833,8 @@ def swa_decode(q, k_cache, v_cache, page_table, seq_lens, window=None, prefix_le
             po = o.data_ptr()
         else:
             po = _need("o", o, qs, _out_of(q, out), q)
-        dims, n = _decode_dims(T, B, Hq, Hkv, d, pages, size, width, (1 << 62) if window is None else int(window),
-                               int(prefix_len), 0.0 if scale is None else float(scale), _dtype_code(dt), int(algo),
+        dims, n = _decode_dims(T, B, Hq, Hkv, d, pages, size, width, (1 << 62) if window is None else _int64(window),
+                               _int64(prefix_len), 0.0 if scale is None else float(scale), _dtype_code(dt), int(algo),
                                _OUT[out])
         ws = _scratch(n, q, stream)
         st = lib().lt2_swa_decode(dims, pq, pkc, pvc, table, lens, po, None if ws is None else ws.data_ptr(), n,
