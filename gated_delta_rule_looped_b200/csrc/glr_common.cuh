@@ -6,54 +6,18 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "f32x2.cuh"
 #include "gdr_common.cuh"
 #include "gdr_tc_common.cuh"
 
 namespace lt2 {
 namespace glr {
 
-constexpr float kLog2e = 1.4426950408889634f;
+using namespace pairs;
 
 // ---- two channels at a time ----------------------------------------------------------------------
-// A pair of fp32 values in one 64-bit register: Blackwell multiplies and adds both in one
-// instruction (f32x2), each half rounded as by itself.  With logits the gates take some 40 scalar
-// operations an element, more than HBM leaves time for; paired they fit under the loads.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack2(float lo, float hi)
-{
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
-{
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b)
-{
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b)
-{
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+// With logits the gates take some 40 scalar operations an element, more than HBM leaves time for; paired they fit
+// under the loads.
 // 2^x of both, rcp of both
 __device__ __forceinline__ f2 ex2_2(f2 v)
 {
@@ -155,7 +119,6 @@ __device__ __forceinline__ float4 floats(F4 v)
     return r;
 }
 __device__ __forceinline__ F4 mul4(F4 x, F4 y) { return {mul2(x.a, y.a), mul2(x.b, y.b)}; }
-__device__ __forceinline__ F4 add4(F4 x, F4 y) { return {add2(x.a, y.a), add2(x.b, y.b)}; }
 __device__ __forceinline__ F4 fma4(F4 x, F4 y, F4 z) { return {fma2(x.a, y.a, z.a), fma2(x.b, y.b, z.b)}; }
 // The decays of N fours of logits.
 template <int N>
@@ -390,18 +353,6 @@ __device__ __forceinline__ f2 carry_into(const uint64_t* maps, const uint32_t* c
 }
 
 // ---- staging a tile -----------------------------------------------------------------------------
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // A warp's ROWS x CB elements of a [.][d] tensor from `g` (the warp's first row, channel 0 of the tile) to
 // shared memory; rows from `rows` on and channels from `chans` on become 0.  Rows are packed, in HALVES
 // interleaved runs: with two, row i of the first half lies beside row i of the second, so that two half warps that

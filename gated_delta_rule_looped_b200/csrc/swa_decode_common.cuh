@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "cache_launch.h"
+#include "f32x2.cuh"
 #include "gdr_common.cuh"
 #include "lt2_api_common.h"
 #include "sm100_primitives.cuh"
@@ -20,7 +21,8 @@
 namespace lt2 {
 namespace swad {
 
-constexpr float kLog2e = 1.4426950408889634f;
+using namespace pairs;
+
 // Blocks of 64 keys whose products the tensor core adds up in a shared prefix before the sum is rounded (a run).
 constexpr int kPrefixRun = 4;
 
@@ -33,13 +35,6 @@ struct Params {
     float* acc;            // [rows][slots][d]: sum of 2^(x - max) v
     float* between;        // [CTA][128 columns][128 rows]: the shared prefix's sums between two runs of blocks, or null
 };
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Weights p >= 0 as three bf16 numbers whose sum is p exactly, all 24 bits of it: p a little lessened (kLess) and cut to
 // 8 bits, the rest treated the same way, and what is left then, which has 8 bits at most.  Lessening by one or two

@@ -23,7 +23,7 @@
 //
 // 4 x 64 sequences of 16 heads over 4, 32,768 shared tokens, and up to 1,500 of their own: 287 us in all.  With two parts
 // of P (the second rounded) and one run it takes 226, and the outputs are twice as far from those of fp32 arithmetic (their
-// bf16 roundings fall the other way 5 times as often); the third part costs 36 us, the runs 25 (their sums added by read and
+// bf16 roundings fall the other way 4 times as often); the third part costs 36 us, the runs 25 (their sums added by read and
 // write instead of in place: 42; runs of 16 blocks in place of 4: 15).  The softmax's own chain per block is what the kernel waits for.  Eight
 // softmax warps spilled their registers and took longer.  Every sequence on its own from HBM: 2,595 us in all.
 #include <cuda.h>
@@ -103,36 +103,6 @@ constexpr uint32_t ID_PV = idesc_bf16_f32(kBM, 128, 0, 1);
 // `words`: where the barriers lie
 __device__ __forceinline__ uint32_t bar_addr(uint32_t words, uint32_t i) { return words + OFF_BAR + 8u * i; }
 
-// A pair of fp32 values in one 64-bit register, multiplied and added in one instruction.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack2(float lo, float hi)
-{
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
-{
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b)
-{
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b)
-{
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
