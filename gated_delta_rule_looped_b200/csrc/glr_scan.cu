@@ -4,7 +4,8 @@
 // each output once; what the tiles exchange is 12 bytes per channel and 64 tokens.
 //
 // A tile's time is a chain of latencies, in cycles as measured inside the kernel: its ticket 1,100, its rows 2,700, its
-// maps 2,800, its carry 2,200, its second half 800.  So three CTAs per SM share it, and a small call takes a few such
+// maps 2,800, its carry 2,200, its second half 800.  So three CTAs per SM share it
+// (for which a thread keeps up to 48 bytes in local memory), and a small call takes a few such
 // chains (16 units of 2,048 x 128 bf16 with logits: 16.4 us, where HBM would take 5).  CTAs that stay and load ahead
 // hold tickets that others wait for, and were slower (30 us); where there are channels enough, glr_stream.cu needs
 // no such waits.

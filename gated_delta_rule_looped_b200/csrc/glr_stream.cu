@@ -10,7 +10,7 @@
 // Eight warps work on the tokens; a ninth passes the state over the groups' maps (glr_tile.cuh) and describes the
 // tiles to come.  The eight do the first half of the next tile before the second half of the present one,
 // and each copies its own rows two tiles ahead: loads and hand-overs run under the arithmetic, whose latency at 18 warps per
-// SM bounds the kernel with logits (35 instructions an element on 54 % of the issue slots; 4 x 4 x 16 units of 8,192 x 128
+// SM (two CTAs, up to 44 bytes of a thread in local memory) bounds the kernel with logits (35 instructions an element on 54 % of the issue slots; 4 x 4 x 16 units of 8,192 x 128
 // bf16: 470 us with logits, 372 us with decays as values, where HBM's copy rate would take 327).
 #include <cuda_runtime.h>
 

@@ -24,8 +24,8 @@ __device__ __forceinline__ float seen(float m, float l) { return l != l && m == 
 // CTA = (loop, sequence, key head, 16 of its query heads) x one split.  A warp of W takes every W-th tile of 16
 // keys through a ring of its own (asynchronous copies, no barrier with the other warps): S = Q K^T with
 // Q in registers, P = 2^(S - m), O += P V.  With at most 16 query rows the tensor core is far from busy;
-// what counts is bytes in flight (8 KB per warp and stage at d = 128; two stages and three CTAs per SM read 5.6 TB/s of
-// 4 x 64 x 16 windows of 512, 194 us, three stages and two CTAs 5.2 TB/s).  A warp looks 32 tiles' pages up at once (4 x
+// what counts is bytes in flight (8 KB per warp and stage at d = 128; two stages and three CTAs per SM read 5.9 TB/s of
+// 4 x 64 x 16 windows of 512, 182 us, three stages and two CTAs 5.0 TB/s, 216 us).  A warp looks 32 tiles' pages up at once (4 x
 // 32 x 4 key heads of 64: 140 us, page by page 162).  P enters the
 // product as three bf16 numbers, which hold all its bits (swa_decode_common.cuh).  A group of up to 8 heads leaves the
 // lower half of the 16 rows empty (R = 1): there the second parts take it, beside the first ones, and O is the sum of
@@ -589,7 +589,7 @@ DecodePlan plan_decode(const DecodeCall& c)
     plan.seqs_per_tile = 1;
     // The keys a sequence may have, as far as the host can tell: splits of 512 at least (a split costs a second
     // launch and its partial results; 128 on CUDA cores, which take longer for a key, and 64 gained nothing), and no
-    // more CTAs than 16 per SM (4 x 48 ragged sequences of up to 16,384 keys: 8 per SM 741 us, 16 698, 32 708).
+    // more CTAs than 16 per SM (4 x 48 ragged sequences of up to 16,384 keys: 8 per SM 648 us, 16 620, 32 627).
     int64_t most = c.max_pages << c.page_shift;
     // A shared prefix: tiles of as many whole sequences as 128 query rows hold, split so that each SM has two CTAs and
     // a CTA four blocks of keys at least.  It pays from the second sequence on: a tile of any size reads the

@@ -14,11 +14,12 @@
 //     O += P V_j            three times: P as three bf16 numbers, all 24 bits of the weights; A from tensor memory,
 //                           the third one's from shared memory
 // The tensor core cuts every sum to fp32 instead of rounding it, towards zero each time: over 57 blocks with twelve sums each
-// O lost 2^-15 of itself.  So after every four blocks (a run) O goes to global memory, where it is added
+// O lost about 2^-15 of itself.  So after every four blocks (a run) O goes to global memory, where it is added
 // to the runs before rounded to nearest, and starts from zero.  O, m and the row sums go out as a partial result.
 //
 // Warps: 0 producer, 1 MMA issuer, 2-5 softmax (a query row per thread).  113 KB of shared memory and 256
-// TMEM columns: two CTAs per SM, one's softmax under the other's products.  Every wait is bounded; on a
+// TMEM columns, 168 registers (60 bytes of a thread are in local memory around the rare calls): two CTAs per SM, one's
+// softmax under the other's products.  Every wait is bounded; on a
 // timeout the CTA records it, drains its copies and MMAs, frees TMEM and exits.
 //
 // 4 x 64 sequences of 16 heads over 4, 32,768 shared tokens, and up to 1,500 of their own: 287 us in all.  With two parts
