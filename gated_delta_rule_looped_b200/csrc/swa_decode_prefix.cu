@@ -25,8 +25,9 @@
 // 4 x 64 sequences of 16 heads over 4, 32,768 shared tokens, and up to 1,500 of their own: 287 us in all.  With two parts
 // of P (the second rounded) and one run it takes 226, and the outputs are twice as far from those of fp32 arithmetic (their
 // bf16 roundings fall the other way 4 times as often); the third part costs 36 us, the runs 25 (their sums added by read and
-// write instead of in place: 42; runs of 16 blocks in place of 4: 15).  The softmax's own chain per block is what the kernel waits for.  Eight
-// softmax warps spilled their registers and took longer.  Every sequence on its own from HBM: 2,595 us in all.
+// write instead of in place: 42; runs of 16 blocks in place of 4: 15).  The softmax's own chain per block is what the
+// kernel waits for.  Eight softmax warps spilled their registers and took longer.  Every sequence on its own from
+// HBM: 2,595 us in all.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -334,7 +335,8 @@ swa_decode_prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
                 const uint32_t vt = sb + OFF_V + (j & 1) * KV_STAGE;
                 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    umma_f16_tmem_a(tmem + TM_O, tmem + TM_P + 32 + 8 * k, smem_desc_sw128(vt + k * 2048, KV_PANEL, 1024), ID_PV, 1u);
+                    umma_f16_tmem_a(tmem + TM_O, tmem + TM_P + 32 + 8 * k, smem_desc_sw128(vt + k * 2048, KV_PANEL, 1024),
+                                    ID_PV, 1u);
                 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     umma_f16(tmem + TM_O, smem_desc_sw128(sb + OFF_P + k * 32, 16, 1024),
